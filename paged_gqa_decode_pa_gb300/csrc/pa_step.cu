@@ -782,10 +782,11 @@ extern "C" int pa_build_slots(const pa_shape* shape, const int32_t* cache_seqlen
   // a step of few sequences and rows fits one small CTA
   if (a.B <= kSlotThreadsSmall && a.T <= kSlotRows)
     return launch(pa_slots_kernel<kSlotThreadsSmall>, dim3(1), kSlotThreadsSmall, slot_smem(a.B), st, a);
-  const size_t smem = slot_smem(a.B);
-  if (smem > 48 * 1024 && !allow_slot_smem()) return PA_ERR_CUDA;
+  // (in every call: what a launch may take without it is 48 KB less the kernel's
+  // own variables)
+  if (!allow_slot_smem()) return PA_ERR_CUDA;
   const int ctas = std::max(1, std::min(kSlotMaxCtas, (a.T + kSlotRows - 1) / kSlotRows));
-  return launch(pa_slots_kernel<kSlotThreads>, dim3(ctas), kSlotThreads, smem, st, a);
+  return launch(pa_slots_kernel<kSlotThreads>, dim3(ctas), kSlotThreads, slot_smem(a.B), st, a);
 }
 
 extern "C" int pa_cache_write(const pa_shape* shape, const void* k_new, int64_t k_stride, const void* v_new,

@@ -207,6 +207,33 @@ def test_slots_with_a_short_stack_and_a_short_map(B, spare):
     same(run_slots(*case), want)
 
 
+_FRESH = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import numpy as np
+from test_step import plain_slots, run_slots, same
+for B in (2405, 2406, 2457, 2458, 2459):
+    table = np.arange(2 * B, dtype=np.int32).reshape(B, 2)
+    case = ([16] * B, [1] * B, [1] * B, table, np.arange(2 * B, dtype=np.int32), 2 * B - 1, 16, B + 2)
+    same(run_slots(*case), plain_slots(*case, P=2 * B))
+print("done")
+"""
+
+
+@pytest.mark.gpu
+def test_slots_of_batches_whose_sums_take_just_under_48_kb():
+    """In a process that has launched no larger batch: the kernel's shared memory is asked for in every call that needs it
+    (its own variables count too, so from 2406 sequences on)."""
+    import os
+    import subprocess
+    import sys
+
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = _FRESH.format(root=os.path.dirname(tests), tests=tests)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.endswith("done\n"), r.stderr[-2000:]
+
+
 @pytest.mark.gpu
 def test_slots_of_one_long_prompt_and_of_nothing():
     cols, bs = 3000, 32
