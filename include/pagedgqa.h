@@ -589,7 +589,8 @@ int pa_copy_blocks(const pa_shape* shape, void* k_cache, void* v_cache, const in
  * negative lengths, more tokens than its table row holds, held_blocks outside
  * ceil(cache_seqlens[b] / bs) .. max_blocks_per_seq, or rows past total_new
  * (PA_STATUS_BAD_SEQLEN).  A free_count outside 0 .. num_blocks, a stack that
- * overflows, or an id outside the pool sets PA_STATUS_BAD_BLOCK.
+ * overflows, or an id outside the pool (among those that go back, too: it is on
+ * the stack then) sets PA_STATUS_BAD_BLOCK.
  * Of shape, batch, block_size, max_blocks_per_seq and num_blocks are used.
  * The workspace needs its first 256 bytes (zero-filled once; the status word
  * and a CTA count); two calls in flight must not share it.

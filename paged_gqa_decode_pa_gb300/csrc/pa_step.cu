@@ -247,8 +247,14 @@ __global__ void __launch_bounds__(NT) pa_slots_kernel(const SlotArgs a) {
     return at >= count ? pushed((int32_t)(at - count)) : a.free_list[at];
   };
   const int at0 = cta * NT + tid, step = ctas * NT;
-  // pushes: given-back blocks go on top of the stack, by sequence and column
-  for (long long x = at0; x < top - count; x += step) a.free_list[count + x] = pushed((int32_t)x);
+  bool bad_id = false;
+  // pushes: given-back blocks go on top of the stack, by sequence and column; one
+  // outside the pool is reported here, not when it is taken
+  for (long long x = at0; x < top - count; x += step) {
+    const int32_t id = pushed((int32_t)x);
+    bad_id |= id < 0 || id >= a.P;
+    a.free_list[count + x] = id;
+  }
   // pops, by sequence and column
   for (long long x = at0; x < min(all.take, top); x += step) {
     const int b = owner(take, B, (int32_t)x);
@@ -256,7 +262,6 @@ __global__ void __launch_bounds__(NT) pa_slots_kernel(const SlotArgs a) {
   }
   // the slot of each new row, and -1 behind the last sequence's
   const long long nrow = min((long long)a.T, all.rows);
-  bool bad_id = false;
   for (long long x = at0; x < a.T; x += step) {
     int64_t slot = -1;
     if (x < nrow) {

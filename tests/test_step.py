@@ -270,6 +270,30 @@ def test_slots_with_ids_outside_the_pool():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bad", [-1, 8, 2**31 - 1])
+@pytest.mark.parametrize("B", [3, 300])
+def test_slots_report_a_bad_id_that_goes_back(B, bad):
+    """A finished sequence, or a rejected draft, that gives back an id outside the pool: the call that puts it on the
+    stack reports it."""
+    P = max(8, 2 * B)
+    bad = P if bad == 8 else bad
+    for held, lens, col in ((2, 0, 1), (2, 0, 0), (2, 10, 1)):  # all blocks go back, or the second one
+        table = np.full((B, 4), -1, np.int32)
+        table[:, :2] = np.arange(2 * B).reshape(B, 2)
+        table[B - 1, col] = bad
+        free = np.full(P, -1, np.int32)
+        case = ([10] * (B - 1) + [lens], [0] * B, [1] * (B - 1) + [held], table, free, 0, 16, 4)
+        got = run_slots(*case)
+        want = plain_slots(*case, P=P)
+        assert got["status"] == pg.PA_STATUS_BAD_BLOCK and want["status"] == 0
+        del want["status"]
+        same(got, want)
+        # a good id raises nothing
+        table[B - 1, col] = 2 * B - 1
+        same(run_slots(*case), plain_slots(*case, P=P))
+
+
+@pytest.mark.gpu
 def test_slots_agree_with_the_block_manager():
     """The device stack hands out the blocks that the host's manager hands out."""
     bs, cols, P, B = 16, 20, 64, 4
