@@ -576,13 +576,15 @@ __device__ __forceinline__ void pf_softmax(const PfArgs& a, PfPieces<D> it, int 
     const int tok = pc.tok0 + (two ? y * a.tt : 0) + rt;
     const bool row = rt < a.tt && tok < pc.nq;
     const int32_t lim = !row ? 0 : (a.causal ? max(0, min(pc.len, pc.len - pc.nq + tok + 1)) : pc.len);
-    // Keys from here on are hidden from the first row, if from any: of the item, of
-    // this tile.  A NaN or an infinity that V holds there is turned to 0 before the
-    // product, where 0 * it would reach the rows that do not see it, and added at
-    // the end to the rows that do; kMark holds the last piece where one was found
-    // (maybe by the other warpgroup).
-    auto limit_of = [&](int t) { return a.causal ? max(0, min(pc.len, pc.len - pc.nq + t + 1)) : pc.len; };
-    const int32_t lim0 = limit_of(pc.tok0), limy = limit_of(pc.tok0 + (two ? y * a.tt : 0));
+    // Keys from here on are hidden from the item's first row, if from any.  A NaN or
+    // an infinity that V holds there is turned to 0 before the product, where 0 * it
+    // would reach the rows that do not see it, and added at the end to the rows that
+    // do; kMark holds the last piece where one was found (maybe by the other
+    // warpgroup).  V's ring unit serves both tiles, so both clear from the same key
+    // on: were the second tile's warpgroup to leave the keys that all of its rows see,
+    // the first one's stores would race with the second tile's product, and a weight
+    // of 0 there give NaN or not by timing.
+    const int32_t lim0 = a.causal ? max(0, min(pc.len, pc.len - pc.nq + pc.tok0 + 1)) : pc.len;
     const uint32_t mark = u + 2u;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -617,8 +619,8 @@ __device__ __forceinline__ void pf_softmax(const PfArgs& a, PfPieces<D> it, int 
       if (!ok) break;
       // rows past the keys inside the last block: 0 * (what lies there) must
       // be 0, so V is cleared there before the product reads it
-      if (k0 + kKeys > limy) {  // (limy <= pc.keys)
-        const int h0 = max(limy - k0, 0), v0 = min(kKeys, pc.keys - k0);
+      if (k0 + kKeys > lim0) {  // (lim0 <= pc.keys)
+        const int h0 = max(lim0 - k0, 0), v0 = min(kKeys, pc.keys - k0);
         const int v1 = min(kKeys, (v0 + a.bs - 1) / a.bs * a.bs);
         if (h0 < v1) {
           // (V's ring unit was full and read before K's landed, so its barrier's
