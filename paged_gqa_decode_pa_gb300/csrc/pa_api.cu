@@ -957,7 +957,7 @@ struct MapEntry {
   const void* pool;
   const void* pool2;  // the other pool of a map over both (nullptr: one pool)
   int32_t D, Hkv, bs, P, dtype;
-  int32_t tc;         // 1: the tcgen05 split kernel's box (make_pool_map); 2: whole pages (make_page_map)
+  int32_t tc;         // the tcgen05 kernel's box (make_pool_map)
   int32_t rc, swap;   // encode result (a map over both pools may be impossible)
   alignas(64) CUtensorMap map;
 };
@@ -968,12 +968,12 @@ int g_nmaps = 0, g_next_map = 0;
 // pool2 == nullptr: the map of one pool; otherwise the map over both pools
 // (make_kv_map), whose result code is cached too.
 int pool_map(CUtensorMap* out, const void* pool, const void* pool2, const pa_shape* s,
-             int* swap, int tc = 0) {
+             int* swap, bool tc = false) {
   std::lock_guard<std::mutex> lk(g_mu);
   for (int i = 0; i < g_nmaps; ++i) {
     const MapEntry& e = g_maps[i];
     if (e.pool == pool && e.pool2 == pool2 && e.D == s->head_dim && e.Hkv == s->num_kv_heads &&
-        e.bs == s->block_size && e.P == s->num_blocks && e.dtype == s->dtype && e.tc == tc) {
+        e.bs == s->block_size && e.P == s->num_blocks && e.dtype == s->dtype && e.tc == (int)tc) {
       if (e.rc == PA_OK) {
         *out = e.map;
         if (swap) *swap = e.swap;
@@ -991,9 +991,7 @@ int pool_map(CUtensorMap* out, const void* pool, const void* pool2, const pa_sha
   e.dtype = s->dtype;
   e.tc = tc;
   e.swap = 0;
-  e.rc = pool2     ? make_kv_map(&e.map, pool, pool2, s, &e.swap)
-         : tc == 2 ? make_page_map(&e.map, pool, s)
-                  : make_pool_map(&e.map, pool, s, tc != 0);
+  e.rc = pool2 ? make_kv_map(&e.map, pool, pool2, s, &e.swap) : make_pool_map(&e.map, pool, s, tc);
   if (e.rc != PA_OK && e.rc != PA_ERR_SHAPE) return e.rc;  // encoder failure: not cached
   const int slot = g_nmaps < kMapCache ? g_nmaps++ : (g_next_map++ % kMapCache);
   g_maps[slot] = e;
@@ -1996,9 +1994,11 @@ extern "C" int pa_prefill(const pa_shape* shape, const pa_options* options, cons
   alignas(64) CUtensorMap tmv;
   rc = make_q_map(&tmq, q, shape, q_stride, total_q, p.tt);
   if (rc) return rc;
-  rc = pool_map(&tmk, k_cache, nullptr, shape, nullptr, 2);
+  // encoded in every call, as q's is: in pool_map's few entries a model's layers
+  // would take the places of the decode calls' maps
+  rc = make_page_map(&tmk, k_cache, shape);
   if (rc) return rc;
-  rc = pool_map(&tmv, v_cache, nullptr, shape, nullptr, 2);
+  rc = make_page_map(&tmv, v_cache, shape);
   if (rc) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   PfArgs a = prefill_args(shape, p, cu_seqlens_q, cache_seqlens, total_q, causal);
