@@ -64,7 +64,10 @@ constexpr int kPfThreads = 384;  // two softmax warpgroups; one with the TMA war
 constexpr int kPfRegsSoftmax = 208, kPfRegsRest = 80;
 static_assert(256 * kPfRegsSoftmax + 128 * kPfRegsRest <= kPfThreads * 168, "the split waits for registers forever");
 constexpr uint32_t kPfChunk = 128u * 128u;  // [128 rows][64 dims], 128-byte swizzled
-constexpr uint64_t kPfWaitNs = 2000000000ull;
+constexpr uint64_t kPfWaitNs = 2000000000ull;  // every wait is for a step or two of another role ...
+// ... but the schedule's, which is for a whole piece: up to 2^30 keys, 2^24 steps of
+// about a microsecond.  (It ends at once where another wait has given up.)
+constexpr uint64_t kPfPieceWaitNs = 100000000000ull;
 // The running maximum m need not be the maximum: any m gives the same output as
 // long as no weight 2^(y - m) leaves its type's range.  Raising m rescales O, a
 // round trip to tensor memory and a wait for the products under way.
@@ -167,7 +170,7 @@ struct PfPieces {
   __device__ __forceinline__ bool put(const PfPiece& p) {
     const uint32_t s = n % kPfSlots;
     if (n >= kPfSlots &&
-        !mbar_wait_bounded(bars + PfBars::piece_empty(s), (n / kPfSlots - 1) & 1u, abort, kPfWaitNs))
+        !mbar_wait_bounded(bars + PfBars::piece_empty(s), (n / kPfSlots - 1) & 1u, abort, kPfPieceWaitNs))
       return false;
     const int32_t* src = reinterpret_cast<const int32_t*>(&p);
 #pragma unroll
