@@ -1202,6 +1202,8 @@ def pa_plan_prefill(shape: pa_shape, cu_host, lens_host, total_q: int, causal, n
 
     cu = np.ascontiguousarray(cu_host, dtype=np.int32)
     lens = np.ascontiguousarray(lens_host, dtype=np.int32)
+    if cu.shape != (shape.batch + 1,) or lens.shape != (shape.batch,):
+        raise ValueError("cu_host must be [B + 1] and lens_host [B]")
     cut = np.zeros(4, dtype=np.int32)
     args = (ctypes.byref(shape), cu.ctypes.data, lens.ctypes.data, int(total_q), int(bool(causal)),
             int(num_ctas), int(cta))
