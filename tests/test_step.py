@@ -542,6 +542,30 @@ def test_verify_edges_and_bad_rows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lookup", [False, True])
+def test_verify_draws_after_a_draft_outside_the_vocabulary(lookup):
+    """The draft is rejected, the token comes from max(p - q, 0), or from p where nothing is left of it, and the row of
+    the missing draft holds -1."""
+    V = 4100
+    rng = np.random.default_rng(6)
+    p = rng.random((6, V)).astype(np.float32)
+    q = rng.random((3, V)).astype(np.float32)
+    p /= p.sum(1, keepdims=True)
+    q /= q.sum(1, keepdims=True)
+    p[4] = q[2]  # sequence 2: nothing is left
+    tokens, cu = [V, -1, 1 << 30], [0, 1, 2, 3]
+    us = np.array([0.5, 0.25, 0.75], np.float32)
+    out, acc, st = run_verify(tokens, cu, None if lookup else q, p, np.zeros(3, np.float32), us)
+    want, none = plain_verify(tokens, cu, q, p, np.zeros(3, np.float32), us, lookup)
+    assert st == pg.PA_STATUS_BAD_TOKEN
+    assert acc.tolist() == none.tolist() == [0, 0, 0]
+    assert out.tolist() == want.tolist()
+    assert out[1::2].tolist() == [-1] * 3 and (out[::2] >= 0).all() and (out[::2] < V).all()
+    c = np.cumsum(p[4].astype(np.float64))
+    assert out[4] == int(np.searchsorted(c, 0.75 * c[-1], side="right"))
+
+
+@pytest.mark.gpu
 def test_verify_workspace_serves_batches_of_any_size():
     import torch
 
@@ -645,3 +669,96 @@ def test_a_serving_loop_of_drafts():
             keep = len(keys[b]) - k + int(acc[b])
             del keys[b][keep:], vals[b][keep:]
         lens.copy_(torch.tensor([len(x) for x in keys]))
+
+
+class _Loop:
+    """Four steps of a serving loop whose lengths, held blocks and free count are updated in place."""
+
+    def __init__(self, seed):
+        import torch
+
+        self.B, self.T, H, Hkv, d, self.bs, cols = 300, 9000, 4, 2, 64, 16, 24
+        rng = np.random.default_rng(seed)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        P = self.B * 20
+        self.new = [torch.tensor(rng.integers(0, 50 if s == 0 else 9, self.B), **i32) for s in range(4)]
+        self.qkv = torch.from_numpy(rng.standard_normal((self.T, H + 2 * Hkv, d)).astype(np.float32)).cuda().bfloat16()
+        self.kv = [torch.zeros(P, self.bs, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        self.table, self.free = torch.full((self.B, cols), -1, **i32), torch.arange(P, **i32)
+        self.lens, self.held, self.count = torch.zeros(self.B, **i32), torch.zeros(self.B, **i32), torch.tensor([P], **i32)
+        self.cu = torch.zeros(self.B + 1, **i32)
+        self.out = [torch.zeros(self.T, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        self.lse = [torch.zeros(self.T, H, device="cuda") for _ in range(4)]
+        self.maps = [torch.zeros(self.T, dtype=torch.int64, device="cuda") for _ in range(4)]
+        self.q, k, v = self.qkv[:, :H], self.qkv[:, H:H + Hkv], self.qkv[:, H + Hkv:]
+        self.k, self.v, self.d = k, v, d
+        self.st, self.ws = pg.alloc_workspace_status(), pg.alloc_workspace_prefill(pg.shape_multi(self.q, self.kv[0], self.table))
+        self.start = [x.clone() for x in self.state()]
+
+    def state(self):
+        return [*self.kv, self.table, self.free, self.lens, self.held, self.count]
+
+    def results(self):
+        return [*self.state(), *self.out, *self.lse, *self.maps]
+
+    def reset(self):
+        for x, y in zip(self.state(), self.start):
+            x.copy_(y)
+        for x in self.out + self.lse + self.maps:
+            x.fill_(7)
+
+    def steps(self, between=lambda: None):
+        for s in range(4):
+            pg.pa_build_slots(self.lens, self.new[s], self.held, self.table, self.free, self.count, self.bs, self.cu,
+                              self.maps[s], self.lens, self.held, self.count, self.st)
+            between()
+            pg.pa_cache_write(self.k, self.v, self.maps[s], *self.kv, self.st)
+            between()
+            pg.pa_prefill(self.q, self.cu, True, *self.kv, self.table, self.lens, self.d ** -0.5, self.out[s], self.lse[s],
+                          self.ws)
+            between()
+
+
+@pytest.mark.gpu
+def test_steps_in_place_and_in_flight_together_give_what_they_give_one_by_one():
+    """Lengths, held blocks and the free count are each call's inputs and outputs, and every call follows the one before
+    without a wait of the host: on one stream, in a replayed graph, and two loops on two streams."""
+    import torch
+
+    loops = [_Loop(seed) for seed in (1, 2)]
+    want = []
+    for x in loops:
+        x.reset()
+        x.steps(torch.cuda.synchronize)
+        want.append([t.clone() for t in x.results()])
+        assert int(x.lens.sum()) == sum(int(n.sum()) for n in x.new)
+
+    def compare():
+        torch.cuda.synchronize()
+        for x, w in zip(loops, want):
+            assert pg.pa_read_status(x.st) == 0 and pg.pa_read_status(x.ws) == 0
+            for a, b in zip(x.results(), w):
+                assert torch.equal(a, b)
+
+    streams, graphs = [torch.cuda.Stream() for _ in loops], []
+    for _ in range(10):
+        for x in loops:
+            x.reset()
+        torch.cuda.synchronize()
+        for x, s in zip(loops, streams):
+            with torch.cuda.stream(s):
+                x.steps()
+        compare()
+    for x, s in zip(loops, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            x.steps()
+        graphs.append(g)
+    for _ in range(10):
+        for x in loops:
+            x.reset()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        compare()
