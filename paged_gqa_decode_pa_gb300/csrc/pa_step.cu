@@ -560,6 +560,17 @@ __device__ int accepted_drafts(const VerifyArgs& a, int b, int c0, int k, int* s
   return *s_first;
 }
 
+// u * total rounded down, exactly (u in [0, 1)): a whole number exceeds the
+// product where it exceeds this.  (The product has up to 72 bits; rounded to a
+// double's 53 it may reach a running sum that lies just above it.)
+__device__ __forceinline__ unsigned long long floor_product(float u, unsigned long long total) {
+  const uint32_t bits = __float_as_uint(u), e = bits >> 23;
+  const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const uint32_t shift = 150u - max(e, 1u);  // u = m 2^-shift; 24 or more
+  const unsigned long long hi = __umul64hi(m, total), lo = m * total;
+  return shift < 64u ? hi << (64u - shift) | lo >> shift : (shift < 128u ? hi >> (shift - 64u) : 0ull);
+}
+
 // The first index of the row whose running sum exceeds u * total, from the
 // segment sums (all threads of the block; the answer in *s_pick).
 template <typename T>
@@ -567,7 +578,7 @@ __device__ void pick(const VerifyArgs& a, const Weights<T>& w, const SegSum* sum
                      float u, unsigned long long* s_scan, int* s_pick) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   u = u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f;
-  const double t = (double)u * (double)total;  // below total, which fits a double
+  const unsigned long long t = floor_product(u, total);  // below total
   __shared__ int s_seg;
   __shared__ unsigned long long s_base;
   if (tid == 0) s_seg = -1;
@@ -583,7 +594,7 @@ __device__ void pick(const VerifyArgs& a, const Weights<T>& w, const SegSum* sum
     for (int i = 0; i < warp; ++i) before += s_scan[i];
     for (int i = 0; i < kVerifyWarps; ++i) run += s_scan[i];
     inc += before;
-    if ((double)inc > t && (double)(inc - v) <= t && v) {
+    if (inc > t && inc - v <= t) {
       s_seg = g0 + tid;
       s_base = inc - v;
     }
@@ -607,11 +618,11 @@ __device__ void pick(const VerifyArgs& a, const Weights<T>& w, const SegSum* sum
   if (lane == 0) s_scan[warp] = mine;
   __syncthreads();
   for (int i = 0; i < warp; ++i) base += s_scan[i];
-  if (mine && (double)base <= t && (double)(base + mine) > t) {
+  if (base <= t && base + mine > t) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const unsigned long long inc = base + warp_scan(v[k]);
-      const unsigned hit = __ballot_sync(0xffffffffu, (double)inc > t);
+      const unsigned hit = __ballot_sync(0xffffffffu, inc > t);
       if (hit) {
         if (lane == 0) *s_pick = (int)(i0 + 32 * k + __ffs(hit) - 1);
         break;

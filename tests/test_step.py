@@ -566,6 +566,28 @@ def test_verify_draws_after_a_draft_outside_the_vocabulary(lookup):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shift", [0, 600])
+def test_verify_draws_exactly_at_a_border_of_the_running_sum(shift):
+    """u * sum(w) lies 2^-23 of a step (2^-46) below a running sum: that sum exceeds it.  In 53 bits they are equal."""
+    s = 2.0 ** -46
+    w = [2 ** 45, 2 ** 24 + 2 ** 22, 1, 2 ** 24 - 2 ** 22 - 3, 2 ** 45]  # whole steps, all held by fp32
+    p = np.zeros((4, 700), np.float32)
+    for b in range(4):
+        p[b, shift + np.arange(5) * 11] = np.array(w, np.float64) * s
+    assert all(float(np.float32(x * s)) == x * s for x in w)
+    u = np.float32(0.5 + 2.0 ** -24)
+    t = Fraction(float(u)) * sum(w)
+    assert sum(w[:3]) - t == Fraction(1, 2 ** 23) and float(t) == sum(w[:3])
+    # and the numbers next to it, and one among fp32's subnormals
+    us = np.array([u, np.nextafter(u, np.float32(1)), np.float32(0.5), np.float32(1e-44)], np.float32)
+    args = ([], [0] * 5, None, p, np.zeros(0, np.float32), us)
+    want, _ = plain_verify(*args, True)
+    assert [(x - shift) / 11 for x in want] == [2, 3, 1, 0]
+    out, acc, st = run_verify(*args)
+    assert st == 0 and out.tolist() == want.tolist()
+
+
+@pytest.mark.gpu
 def test_verify_workspace_serves_batches_of_any_size():
     import torch
 
