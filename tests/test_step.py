@@ -784,3 +784,59 @@ def test_steps_in_place_and_in_flight_together_give_what_they_give_one_by_one():
             with torch.cuda.stream(s):
                 g.replay()
         compare()
+
+
+@pytest.mark.gpu
+def test_blocks_whose_offsets_pass_32_bits():
+    """Pools of 4.9 10^9 elements each, blocks at their end: tables, slots, written rows and attention over them."""
+    import torch
+
+    P, bs, Hkv, d, n, H = 300000, 16, 8, 128, 333, 16
+    i32 = dict(dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    kc, vc = (torch.empty(P, bs, Hkv, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    free, count = torch.zeros(P, **i32), torch.tensor([40], **i32)
+    free[:40] = P - 1 - 3 * torch.arange(40, device="cuda")
+    table, new, held = torch.full((1, 64), -1, **i32), torch.tensor([n], **i32), torch.zeros(1, **i32)
+    lens, cu, slots = torch.zeros(1, **i32), torch.zeros(2, **i32), torch.zeros(n, dtype=torch.int64, device="cuda")
+    st = pg.alloc_workspace_status()
+    pg.pa_build_slots(lens, new, held, table, free, count, bs, cu, slots, lens, held, count, st)
+    ids = P - 1 - 3 * np.arange(39, 39 - 21, -1)  # from the top of the stack
+    assert table[0, :21].tolist() == ids.tolist() and count.item() == 19
+    assert slots.tolist() == [int(ids[i // bs]) * bs + i % bs for i in range(n)]
+    k, v = (torch.randn(n, Hkv, d, generator=g, device="cuda").half() for _ in range(2))
+    pg.pa_cache_write(k, v, slots, kc, vc, st)
+    assert torch.equal(kc.view(-1, Hkv, d)[slots], k) and torch.equal(vc.view(-1, Hkv, d)[slots], v)
+    q = torch.randn(n, H, d, generator=g, device="cuda").half()
+    out, ws = torch.zeros_like(q), pg.alloc_workspace_prefill(pg.shape_multi(q, kc, table))
+    pg.pa_prefill(q, cu, True, kc, vc, table, lens, d ** -0.5, out, None, ws)
+    # the same rows in a pool of their own blocks
+    small = [torch.zeros(21, bs, Hkv, d, dtype=torch.float16, device="cuda") for _ in range(2)]
+    for pool, rows in zip(small, (k, v)):
+        pool.view(-1, Hkv, d)[:n] = rows
+    want = torch.zeros_like(q)
+    pg.pa_prefill(q, cu, True, *small, torch.arange(21, **i32)[None].contiguous(), lens, d ** -0.5, want, None, ws)
+    assert torch.equal(out, want)
+    x = torch.einsum("qhd,khd->hqk", q.double(), k.double().repeat_interleave(H // Hkv, 1)) * d ** -0.5
+    x.masked_fill_(torch.ones(n, n, dtype=torch.bool, device="cuda").triu(1), -float("inf"))
+    w, vd = x.softmax(-1), v.double().repeat_interleave(H // Hkv, 1)
+    ref, A = torch.einsum("hqk,khd->qhd", w, vd), torch.einsum("hqk,khd->qhd", w, vd.abs())
+    u = 2.0 ** -11  # a rounding of the output, one of each weight; subnormal weights; fp32's exponentials and sums
+    assert ((out.double() - ref).abs() <= u * (ref.abs() * (1 + u) + A) + n * 2.0 ** -25 * 5 + 2.0 ** -13 * A + 2.0 ** -24).all()
+    assert pg.pa_read_status(st) == 0 and pg.pa_read_status(ws) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "float16"])
+def test_verify_the_largest_vocabulary(dtype):
+    import torch
+
+    V = pg.PA_MAX_VOCAB
+    p = torch.full((3, V), 2.0 ** -24, dtype=getattr(torch, dtype), device="cuda")  # sums to 1
+    us = torch.tensor([0.0, 0.5, 1 - 2.0 ** -24], device="cuda")
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    tokens, acc = torch.full((3,), -9, dtype=torch.int32, device="cuda"), torch.full((3,), -9, dtype=torch.int32, device="cuda")
+    ws = pg.alloc_workspace_verify(3, V)
+    pg.pa_verify_drafts(none, torch.zeros(4, dtype=torch.int32, device="cuda"), None, p, none.float(), us, tokens, acc, ws)
+    assert pg.pa_read_status(ws) == 0
+    assert tokens.tolist() == [0, V // 2, V - 1] and acc.tolist() == [0, 0, 0]
