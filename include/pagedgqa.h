@@ -571,7 +571,7 @@ int pa_copy_blocks(const pa_shape* shape, void* k_cache, void* v_cache, const in
  *   free_list      [num_blocks]             in and out: the stack, its top at
  *                  free_list[*free_count - 1]
  *   cu_seqlens_q   [B + 1] out: running sums of new_lens (pa_prefill's and
- *                  pa_decode_multi's row offsets)
+ *                  pa_decode_multi's row offsets), total_new where they pass it
  *   slots          [total_new] out, int64: row cu_seqlens_q[b] + i holds the
  *                  slot of token cache_seqlens[b] + i of sequence b, which is
  *                  block * bs + row in the block; -1 in the rows of a
@@ -585,7 +585,8 @@ int pa_copy_blocks(const pa_shape* shape, void* k_cache, void* v_cache, const in
  * replays with any lengths that fit it.
  *
  * A sequence that needs more blocks than are left is not served, nor is any
- * later one that needs a block (PA_STATUS_NO_BLOCKS).  Nor is a sequence with
+ * later one that needs a block (PA_STATUS_NO_BLOCKS).  (Its rows stay in
+ * cu_seqlens_q; what an attention call puts there means nothing.)  Nor is a sequence with
  * negative lengths, more tokens than its table row holds, held_blocks outside
  * ceil(cache_seqlens[b] / bs) .. max_blocks_per_seq, or rows past total_new
  * (PA_STATUS_BAD_SEQLEN).  A free_count outside 0 .. num_blocks, a stack that
@@ -625,7 +626,7 @@ int pa_cache_write(const pa_shape* shape, const void* k_new, int64_t k_stride, c
  * pa_cache_write), and row i sees
  *   causal != 0:  keys t < clamp(cache_seqlens[b] - n_q + i + 1, 0, cache_seqlens[b])
  *   causal == 0:  all cache_seqlens[b] keys (e.g. an encoder's cached states)
- * Differences: the products run on tcgen05 tiles of 128 rows x 128 keys, so a
+ * Differences: the products run on tcgen05 tiles of 128 rows x 64 keys, so a
  * long chunk runs at the matrix cores' rate; out has q's type; there is no
  * bound on n_q; lse gives each row's log-sum-exp.
  *   q         [total_q, H, d], q_stride elements from token to token (>= H * d,
@@ -636,8 +637,13 @@ int pa_cache_write(const pa_shape* shape, const void* k_new, int64_t k_stride, c
  * lse = -infinity.  Scores, sums and the accumulator are fp32; the weights
  * are rounded to dt for their product with V.  (In bf16 a row's sums may hold
  * weights up to 2^40 before they are divided, so |V| is to stay below 2^60.)
+ * The accumulator is the tensor core's, which cuts what an addend has below its
+ * last bit, and so an addend below 2^-24 of it altogether.  Over very many keys
+ * that one CTA takes by itself and whose products have one sign, out comes out
+ * too small: by 4 10^-4 of it for 131,072 keys, 3 to 5 10^-3 for a million.
  * What lies in the cache past a row's keys does not matter, NaN and infinity
- * included.
+ * included.  A NaN or an infinity in V that a row sees makes that dim of its out
+ * one, which of them where the key's weight underflows to 0 is not said.
  * A span that is not non-decreasing within [0, total_q] is skipped
  * (PA_STATUS_BAD_SEQLEN); an invalid cache_seqlens[b] makes its rows NaN
  * (same bit); a bad table entry makes the rows that see its keys NaN

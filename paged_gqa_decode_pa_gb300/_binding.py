@@ -69,7 +69,7 @@ EXPORTS = ("pa_workspace_size", "pa_decode", "pa_decode_split", "pa_decode_merge
            "pa_workspace_size_host_async", "pa_decode_multi_host_async",
            "pa_workspace_size_multi_host_async", "pa_launch_plan", "pa_build_slots",
            "pa_cache_write", "pa_prefill", "pa_workspace_size_prefill", "pa_verify_drafts",
-           "pa_plan_prefill",            "pa_workspace_size_verify")
+           "pa_plan_prefill", "pa_workspace_size_verify")
 
 
 class LibraryNotBuilt(RuntimeError):

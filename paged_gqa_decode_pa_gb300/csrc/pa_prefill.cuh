@@ -28,19 +28,25 @@
 //
 // Rounding.  Scores, maxima, sums and O stay in fp32; P is rounded to the
 // storage type for the product (by at most 2^-8 or 2^-11 of a weight, the size
-// of the output's own rounding) while the sum takes the unrounded values.
+// of the output's own rounding; in fp16 a weight below 2^-14 by up to 2^-25, with
+// the largest at 1 or more) while the sum takes the unrounded values.  The tensor
+// core aligns the addends to the accumulator and cuts what lies below its last
+// bit: a product below 2^-24 of it is lost in either type.  (So weights lifted by
+// 2^7 in fp16, to keep small ones from rounding to 0, gave no better an output
+// behind a first key of 2^25 times the others' weight, 3.4 10^-3 off for 131,072
+// keys on one CTA, and prompts took 277 us for 269.)
 //
 // Measured on a GB300 (cuBLAS bf16 1911 TFLOP/s, copy 6768 GB/s): 4096 rows of
 // 24 heads over 32,768 keys, d = 256, bf16: 2.4 ms, 1270 TFLOP/s (products at
 // their rate, the copies of K and V from L2 bound it; long runs are also
 // power-capped, cuBLAS then gives 1730).  Prompts of 2000 tokens, 64 heads, d =
-// 128, fp16: 264 us, 1000 TFLOP/s, tensor pipe 48% active, issue slots 46%: the
+// 128, fp16: 273 us, 960 TFLOP/s, tensor pipe 46% active, issue slots 43%: the
 // hand-overs between scores, softmax and products bound it, and the pieces' starts
 // and ends.  Steps of 128 keys, with one S buffer a tile and the tiles' products
-// in turn, took 258 us there, but 158 us for decode rows beside chunks (152 then;
-// 157 since V is looked over where some row of a tile does not see a key),
-// 47.5 for rows that all see 700 to 2500 keys at d = 64 (44) and 20.4 for single
-// tokens (17.3).  Also slower: half of Q in tensor memory, with one S buffer and P
+// in turn, took 258 us there (265 with 64 then; looking V over for what is hidden
+// took 8 more), but 158 us for decode rows beside chunks (152, and 6 for V), 47.5 for
+// rows that all see 700 to 2500 keys at d = 64 (44) and 20.4 for single tokens
+// (17.3).  Also slower: half of Q in tensor memory, with one S buffer and P
 // beside it (276 us, and 167 for decode rows beside chunks); the next scores
 // loaded before this step's weights are handed over (281, 160); all products
 // issued by one warp (378: its waits and commits, about 700 cycles a step, bound

@@ -30,8 +30,8 @@ constexpr int kPfItemCost = 256;
 constexpr int kPfUnits = 4, kPfUnitsOneTile = 3;
 // The least share of a CTA, in units: below it, cutting an item costs more (a
 // second state, the merge) than it saves; single tokens 640, 512, 384 keys:
-// 19.7, 18.8, 18.1 us.  (More than twice 128 keys, so that no share of an item
-// but its first falls inside one tile.)
+// 19.7, 18.8, 18.1 us when measured (17.3 now).  (More than twice 128 keys, so
+// that no share of an item but its first falls inside one tile.)
 constexpr int kPfMinShare = 384 * kPfUnits;
 
 struct PfArgs {

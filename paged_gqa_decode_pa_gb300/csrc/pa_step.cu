@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kWriteThreads) pa_cache_write_kernel(const Wri
 // segments of kSegment values, a warp per segment; the last CTA of the
 // sequence to finish scans the segment sums, finds the crossing segment and
 // reads it once more (from L2).  256 rows of 131,071 fp32 values and 120 draft
-// rows (197 MB): 50 us, 4.0 TB/s, bound by the latency of its 4-byte loads (rows
+// rows (197 MB): 49 us, 4.0 TB/s, bound by the latency of its 4-byte loads (rows
 // of an odd length are aligned to one value only); 127 us with 64-bit shifts per
 // value.  Bulk copies into shared memory took 64 us (16 to 24 warps cannot keep
 // up with the sums), a kernel of its own for the accepted counts 49 us, with
